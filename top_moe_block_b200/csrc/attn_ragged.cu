@@ -100,6 +100,12 @@ struct Cfg {
   static constexpr int RAW_OFF = D == 128 ? ATOM : TILE;
   static constexpr int SLOT = TILE + (F8 && D == 64 ? kKeys * D : 0);
   static constexpr int RING = D == 128 ? 5 : 8;
+  // Barriers of the raw tiles, position p's at p % RAWS.  A parity wait tells a phase from its neighbours
+  // only, so whoever waits at p must have seen p - RAWS land.  The two expanding groups take positions in
+  // turn: with an odd ring and a barrier a slot, the slot's last use is the other group's, and a copy
+  // that overtakes others would let a tile be expanded before it is there.
+  static constexpr int RAWS = RING % 2 ? 2 * RING : RING;
+  static constexpr int FULLS = F8 ? RAWS : RING;       // barriers that the copies arrive on
   static constexpr int WARPS = F8 ? 16 : 12;
   static constexpr int THREADS = 32 * WARPS;
   // registers: the launch gives every thread 168 (E4M3: 128); the first warpgroup
@@ -484,8 +490,8 @@ __global__ void __launch_bounds__(Cfg<D, F8>::THREADS, 1)
   uint64_t* seg_empty = seg_full + kSegs;    // [kSegs]
   uint64_t* sm_sync = seg_empty + kSegs;     // the softmax warps among themselves
   uint64_t* mdrain = sm_sync + 1;            // the MMA thread's last commit
-  uint64_t* raw_full = mdrain + 1;           // [RING] E4M3 bytes are there
-  Seg* segs = reinterpret_cast<Seg*>(raw_full + (F8 ? RING : 0));   // [kSegs]
+  uint64_t* raw_full = mdrain + 1;           // [RAWS] E4M3 bytes are there
+  Seg* segs = reinterpret_cast<Seg*>(raw_full + (F8 ? C::RAWS : 0));   // [kSegs]
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(segs + kSegs);
   int* s_last = reinterpret_cast<int*>(tmem_slot + 1);
   __shared__ long long s_sum[C::WARPS], s_base, s_weight;
@@ -504,8 +510,8 @@ __global__ void __launch_bounds__(Cfg<D, F8>::THREADS, 1)
     for (int s = 0; s < RING; ++s) {
       mbar_init(&kv_full[s], F8 ? kCvtWarps : 1);
       mbar_init(&kv_empty[s], 1);
-      if (F8) mbar_init(&raw_full[s], 1);
     }
+    for (int s = 0; F8 && s < C::RAWS; ++s) mbar_init(&raw_full[s], 1);
     for (int s = 0; s < kSegs; ++s) {
       mbar_init(&seg_full[s], 1);
       mbar_init(&seg_empty[s], C::WARPS - 2);   // every warp but the walker and the idle one
@@ -669,13 +675,14 @@ __global__ void __launch_bounds__(Cfg<D, F8>::THREADS, 1)
           const uint32_t slot = pos % RING;
           if (!__all_sync(0xffffffffu, mbar_wait(&kv_empty[slot], ((pos / RING) & 1) ^ 1u, wc))) return false;
           const uint32_t boxes = __popc(__ballot_sync(0xffffffffu, page != kNoBox));
-          if (lane == 0) mbar_arrive_expect_tx(&full[slot], boxes * (uint32_t)(box * ROW));
+          uint64_t* landed = &full[pos % C::FULLS];
+          if (lane == 0) mbar_arrive_expect_tx(landed, boxes * (uint32_t)(box * ROW));
           __syncwarp();
           if (page != kNoBox) {
             uint8_t* dst = sKV + slot * C::SLOT + (F8 ? C::RAW_OFF : my_sub * C::ATOM) + my_box * box * ROW;
             const int key = ((sg.kt0 + j) << 7) + my_box * box;
-            if (PAGED) tma_load_3d(dst, map, &full[slot], my_sub * 64, (sg.g << p.page_shift) + (key & (P - 1)), page);
-            else tma_load_3d(dst, map, &full[slot], my_sub * 64, sg.g, sg.first + key);
+            if (PAGED) tma_load_3d(dst, map, landed, my_sub * 64, (sg.g << p.page_shift) + (key & (P - 1)), page);
+            else tma_load_3d(dst, map, landed, my_sub * 64, sg.g, sg.first + key);
           }
           ++pos;
           return true;
@@ -693,7 +700,7 @@ __global__ void __launch_bounds__(Cfg<D, F8>::THREADS, 1)
       // every copy started must land before the CTA may exit
       for (int h = 0; h < 2; ++h)
         if (q_use[h]) mbar_drain(&q_full[h], (q_use[h] - 1) & 1, p.status);
-      for (uint32_t q = pos > RING ? pos - RING : 0; q < pos; ++q) mbar_drain(&full[q % RING], (q / RING) & 1, p.status);
+      for (uint32_t q = pos > RING ? pos - RING : 0; q < pos; ++q) mbar_drain(&full[q % C::FULLS], (q / C::FULLS) & 1, p.status);
     } else if (warp == 1) {
       // ---------------- MMA issuer: one thread (the warp reads the segments together)
       const bool leader = elect_one();
@@ -1182,6 +1189,7 @@ __global__ void __launch_bounds__(Cfg<D, F8>::THREADS, 1)
       // kCvtWarps warps a tile, so that several tiles are under way: what a tile takes is
       // mostly latency (its barrier, shared memory, the proxy fence)
       constexpr int GROUPS = 4 / kCvtWarps;
+      static_assert(C::RAWS % GROUPS == 0, "a barrier's uses are all one group's");
       constexpr int CPR = D / 16;             // 16-byte chunks of a raw row
       constexpr int RPI = 32 / CPR;           // rows a warp takes at once
       constexpr int ROUNDS = kKeys / (RPI * kCvtWarps), BATCH = 1;
@@ -1199,7 +1207,7 @@ __global__ void __launch_bounds__(Cfg<D, F8>::THREADS, 1)
           const bool is_k = q == 0 || ((q & 1) && q < 2 * n - 1);
           const int j = is_k ? (q + 1) >> 1 : (q == 2 * n - 1 ? n - 1 : (q >> 1) - 1);
           const uint32_t slot = pos % RING;
-          ok = __all_sync(0xffffffffu, mbar_wait(&raw_full[slot], (pos / RING) & 1, wc));
+          ok = __all_sync(0xffffffffu, mbar_wait(&raw_full[pos % C::RAWS], (pos / C::RAWS) & 1, wc));
           if (!ok) break;
           const int key0 = (sg.kt0 + j) << 7;
           const bool edge = key0 < sg.lo || key0 + kKeys > sg.hi;
