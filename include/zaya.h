@@ -356,10 +356,12 @@ typedef struct zaya_paged_kv {
  *  positions    [T] out: its position in its row; token_row [T] out: its row;
  *               all three -1 behind the last row.
  * All or nothing: where a length is negative, a row with drop_len has a
- * ctx_len, the tokens exceed T or max_pages * page_size, or the stack runs
- * short, ZAYA_ERR_DEVICE_RANGE is recorded, the table and the stack stay as
- * they are, cu_new is 0 throughout (seq_len = ctx_len) and every token's slot
- * is -1.  An entry of -1 (no page) where a page is looked for is handed on as
+ * ctx_len, the tokens exceed T or max_pages * page_size, the stack runs
+ * short, or a page id that the step drops, pops or goes on with is outside
+ * the pool, ZAYA_ERR_DEVICE_RANGE is recorded, the table and the stack stay as
+ * they are (places of free_list behind *n_free_in are no part of the stack and
+ * may be written), cu_new is 0 throughout (seq_len = ctx_len) and every
+ * token's slot is -1.  An entry of -1 (no page) where a page is looked for is handed on as
  * it is: its tokens get negative slots, which are not stored, and attention
  * that needs it records the fault.  Arrays must not overlap except as stated. */
 int zaya_paged_plan(int32_t B, int32_t T, const int32_t* ctx_len, const int32_t* new_len, const int32_t* drop_len,

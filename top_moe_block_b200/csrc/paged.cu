@@ -16,6 +16,10 @@
 // takes two launches over the whole GPU, since dropped pages must be on the
 // stack before they are handed out again: 1024 rows and 131072 tokens in
 // 14.6 us, against 29 us in one cluster of eight CTAs.
+// All or nothing: every page id that the step drops, pops or goes on with is looked
+// at before any is handed out.  Until then only places of the stack above its top are
+// written, and the second launch records no fault of its own: the status word that
+// its CTAs read is the first launch's.
 //
 // Store.  kv[slot] = (k, v) of every token with a slot, as bf16 or as E4M3
 // bytes (nearest, ties to even, saturating).  A thread moves 16-byte chunks of K
@@ -93,7 +97,7 @@ constexpr int kPlanOneCta = 2 * kPlanThreads;
 
 enum PlanPart {
   PLAN_ALL,    // everything, one CTA
-  PLAN_DROP,   // many CTAs: the dropped pages go on the stack
+  PLAN_DROP,   // many CTAs: the page ids are checked, the dropped pages go above the stack's top
   PLAN_REST    // many CTAs, behind PLAN_DROP: the table, the lengths, the tokens
 };
 
@@ -112,6 +116,7 @@ __global__ void __launch_bounds__(kPlanThreads) paged_plan_kernel(const PagedPla
   // n_free_out may be n_free_in: its old value reaches PLAN_REST through the workspace
   const int n_free = PART == PLAN_REST ? *p.n_free_old : *p.n_free_in;
 
+  auto outside = [&](int id) { return id < -1 || id >= p.n_pages; };   // -1, the mark of no page, is handed on like a page
   uint32_t v[3] = {0, 0, 0}, mine[kPlanRows][3];
   bool bad = status_peek(p.status) != 0;   // a fault earlier in the step: nothing is handed out
 #pragma unroll
@@ -154,8 +159,47 @@ __global__ void __launch_bounds__(kPlanThreads) paged_plan_kernel(const PagedPla
   bad = __syncthreads_or(bad);
   if (PART == PLAN_DROP && me == 0) *p.n_free_old = n_free;
 
+  // a token's row and position, and the id of its page: pages the row already held come from
+  // its table, new ones from the stack (another thread may be writing their table entries)
+  auto token = [&](int t, int& b, int& pos) {
+    b = find_row(s_cu, p.B, (uint32_t)t);
+    const int ctx = p.ctx_len[b];
+    pos = ctx + (int)((uint32_t)t - s_cu[b]);
+    const int have = (int)(((long long)ctx + pm) >> sh), j = pos >> sh;
+    return j < have ? p.block_table[(size_t)b * p.max_pages + j] : p.free_list[top - 1 - (s_need[b] + (uint32_t)(j - have))];
+  };
+  constexpr int kMine = kPlanOneCta / kPlanThreads;
+  int row[kMine], pos[kMine], id[kMine];   // PLAN_ALL: this thread's tokens
+  if (PART != PLAN_REST && !bad) {
+    auto goes_on = [&](int b) {   // the page that holds some of row b's tokens and takes more
+      const int ctx = b < p.B ? p.ctx_len[b] : 0;
+      return (ctx & pm) && p.new_len[b] > 0 ? p.block_table[(size_t)b * p.max_pages + (ctx >> sh)] : -1;
+    };
+    const int first = PART == PLAN_DROP ? goes_on(me) : -1;   // on its way beside the dropped ones
+    for (uint32_t k = me; k < total[2]; k += all) {   // former requests' pages go above the stack's top
+      const int b = find_row(s_gone, p.B, k);
+      const int x = p.block_table[(size_t)b * p.max_pages + (k - s_gone[b])];
+      bad |= outside(x);
+      p.free_list[(uint32_t)n_free + k] = x;
+    }
+    if (PART == PLAN_ALL) {   // every page popped or gone on with is some token's
+      if (total[2]) __syncthreads();
+#pragma unroll
+      for (int u = 0; u < kMine; ++u) {
+        const int t = tid + u * kPlanThreads;
+        row[u] = pos[u] = id[u] = -1;
+        if ((uint32_t)t < total[0]) id[u] = token(t, row[u], pos[u]);
+        bad |= outside(id[u]);
+      }
+    } else {
+      for (long long k = (long long)top - total[1] + me; k < n_free; k += all) bad |= outside(p.free_list[k]);
+      bad |= outside(first);
+      for (int b = me + all; b < p.B; b += all) bad |= outside(goes_on(b));
+    }
+    bad = __syncthreads_or(bad);
+  }
   if (bad) {   // nothing happens: no token has a slot, the table and the stack stay as they are
-    if (me == 0) set_status(p.status, ZAYA_ERR_DEVICE_RANGE);   // keeps an earlier fault
+    if (PART != PLAN_REST && tid == 0) set_status(p.status, ZAYA_ERR_DEVICE_RANGE);   // keeps an earlier fault
     if (PART == PLAN_DROP) return;
     if (me == 0) {
       *p.n_free_out = n_free;
@@ -172,19 +216,7 @@ __global__ void __launch_bounds__(kPlanThreads) paged_plan_kernel(const PagedPla
     }
     return;
   }
-
-  auto checked = [&](int id) {   // -1, the mark of no page, is handed on like a page
-    if (id < -1 || id >= p.n_pages) set_status(p.status, ZAYA_ERR_DEVICE_RANGE);
-    return id;
-  };
-  if (PART != PLAN_REST) {
-    for (uint32_t k = me; k < total[2]; k += all) {   // former requests' pages go on the stack
-      const int b = find_row(s_gone, p.B, k);
-      p.free_list[(uint32_t)n_free + k] = checked(p.block_table[(size_t)b * p.max_pages + (k - s_gone[b])]);
-    }
-    if (PART == PLAN_DROP) return;
-    __syncthreads();
-  }
+  if (PART == PLAN_DROP) return;
   // From here on page ids of the step come from the stack, and the table is written at
   // entries of dropped pages and of new ones only, each by one thread.
   if (me == 0) *p.n_free_out = (int)(top - total[1]);
@@ -196,27 +228,27 @@ __global__ void __launch_bounds__(kPlanThreads) paged_plan_kernel(const PagedPla
   for (uint32_t k = me; k < total[1]; k += all) {   // new pages come off it
     const int b = find_row(s_need, p.B, k);
     const int have = (int)(((long long)p.ctx_len[b] + pm) >> sh);
-    p.block_table[(size_t)b * p.max_pages + have + (k - s_need[b])] = checked(p.free_list[top - 1 - k]);
+    p.block_table[(size_t)b * p.max_pages + have + (k - s_need[b])] = p.free_list[top - 1 - k];
   }
   for (int b = me; b <= p.B; b += all) {
     p.cu_new[b] = (int)s_cu[b];
     if (b < p.B) p.seq_len[b] = p.ctx_len[b] + p.new_len[b];
   }
-  for (int t = me; t < p.T; t += all) {
-    int slot = -1, pos = -1, b = -1;
-    if ((uint32_t)t < total[0]) {
-      b = find_row(s_cu, p.B, (uint32_t)t);
-      const int ctx = p.ctx_len[b];
-      pos = ctx + (int)((uint32_t)t - s_cu[b]);
-      const int have = (int)(((long long)ctx + pm) >> sh), j = pos >> sh;
-      // pages the row already held come from its table, new ones from the stack
-      // (another thread may still be writing their table entries)
-      const int id = j < have ? p.block_table[(size_t)b * p.max_pages + j] : p.free_list[top - 1 - (s_need[b] + (uint32_t)(j - have))];
-      slot = checked(id) >= -1 && id < p.n_pages ? id * (pm + 1) + (pos & pm) : -1;
-    }
-    p.slot_map[t] = slot;
-    p.positions[t] = pos;
+  auto put = [&](int t, int b, int at, int page) {
+    p.slot_map[t] = b < 0 ? -1 : page * (pm + 1) + (at & pm);
+    p.positions[t] = at;
     p.token_row[t] = b;
+  };
+  if (PART == PLAN_ALL) {
+#pragma unroll
+    for (int u = 0; u < kMine; ++u)
+      if (tid + u * kPlanThreads < p.T) put(tid + u * kPlanThreads, row[u], pos[u], id[u]);
+  } else {
+    for (int t = me; t < p.T; t += all) {
+      int b = -1, at = -1;
+      const int page = (uint32_t)t < total[0] ? token(t, b, at) : -1;
+      put(t, b, at, page);
+    }
   }
 }
 
@@ -286,8 +318,8 @@ int launch_paged_plan(const PagedPlanParams& p, int num_sms, cudaStream_t st) {
     return launch_k(kern, dim3(grid), dim3(kPlanThreads), smem, st, nullptr, 0, p) == cudaSuccess;
   };
   if (paged_plan_launches(p.T) == 1) return go(paged_plan_kernel<PLAN_ALL>, 1) ? ZAYA_OK : ZAYA_ERR_CUDA;
-  const long long entries = (long long)p.B * p.max_pages;
-  const int drop = p.drop_len ? (int)std::min<long long>(num_sms, (entries + kPlanThreads - 1) / kPlanThreads) : 1;
+  const long long ids = (p.drop_len ? (long long)p.B * p.max_pages : 0) + p.B + (p.T >> p.page_shift);   // at most
+  const int drop = (int)std::min<long long>(num_sms, (ids + kPlanThreads - 1) / kPlanThreads);
   const int rest = std::min(num_sms, (p.T + kPlanThreads - 1) / kPlanThreads);
   return go(paged_plan_kernel<PLAN_DROP>, drop) && go(paged_plan_kernel<PLAN_REST>, rest) ? ZAYA_OK : ZAYA_ERR_CUDA;
 }
