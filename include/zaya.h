@@ -361,9 +361,11 @@ typedef struct zaya_paged_kv {
  * the pool, ZAYA_ERR_DEVICE_RANGE is recorded, the table and the stack stay as
  * they are (places of free_list behind *n_free_in are no part of the stack and
  * may be written), cu_new is 0 throughout (seq_len = ctx_len) and every
- * token's slot is -1.  An entry of -1 (no page) where a page is looked for is handed on as
- * it is: its tokens get negative slots, which are not stored, and attention
- * that needs it records the fault.  Arrays must not overlap except as stated. */
+ * token's slot is -1.  Only a dropped entry may be -1 (no page): it goes on the
+ * stack as it is, and a row that gets it in the same step has negative slots
+ * there, which are not stored.  In a page that a row goes on with, or on the
+ * stack from an earlier step (a request dropped twice, or at more tokens than it
+ * held), -1 is outside the pool.  Arrays must not overlap except as stated. */
 int zaya_paged_plan(int32_t B, int32_t T, const int32_t* ctx_len, const int32_t* new_len, const int32_t* drop_len,
                     int32_t* block_table, int32_t max_pages, int32_t* free_list, int32_t n_pages,
                     const int32_t* n_free_in, int32_t* n_free_out, int32_t page_size, int32_t* cu_new,

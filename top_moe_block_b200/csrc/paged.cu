@@ -116,7 +116,9 @@ __global__ void __launch_bounds__(kPlanThreads) paged_plan_kernel(const PagedPla
   // n_free_out may be n_free_in: its old value reaches PLAN_REST through the workspace
   const int n_free = PART == PLAN_REST ? *p.n_free_old : *p.n_free_in;
 
-  auto outside = [&](int id) { return id < -1 || id >= p.n_pages; };   // -1, the mark of no page, is handed on like a page
+  // Ids are pages, but that a dropped entry may be -1 (no page).  On the stack of an earlier step or
+  // in the page a row goes on with, -1 would be a page that its tokens' keys never reach.
+  auto outside = [&](int id, int least = 0) { return id < least || id >= p.n_pages; };
   uint32_t v[3] = {0, 0, 0}, mine[kPlanRows][3];
   bool bad = status_peek(p.status) != 0;   // a fault earlier in the step: nothing is handed out
 #pragma unroll
@@ -161,25 +163,27 @@ __global__ void __launch_bounds__(kPlanThreads) paged_plan_kernel(const PagedPla
 
   // a token's row and position, and the id of its page: pages the row already held come from
   // its table, new ones from the stack (another thread may be writing their table entries)
-  auto token = [&](int t, int& b, int& pos) {
+  auto token = [&](int t, int& b, int& pos, bool& dropped) {
     b = find_row(s_cu, p.B, (uint32_t)t);
     const int ctx = p.ctx_len[b];
     pos = ctx + (int)((uint32_t)t - s_cu[b]);
     const int have = (int)(((long long)ctx + pm) >> sh), j = pos >> sh;
-    return j < have ? p.block_table[(size_t)b * p.max_pages + j] : p.free_list[top - 1 - (s_need[b] + (uint32_t)(j - have))];
+    const uint32_t at = top - 1 - (s_need[b] + (uint32_t)(j - have));
+    dropped = j >= have && at >= (uint32_t)n_free;
+    return j < have ? p.block_table[(size_t)b * p.max_pages + j] : p.free_list[at];
   };
   constexpr int kMine = kPlanOneCta / kPlanThreads;
   int row[kMine], pos[kMine], id[kMine];   // PLAN_ALL: this thread's tokens
   if (PART != PLAN_REST && !bad) {
     auto goes_on = [&](int b) {   // the page that holds some of row b's tokens and takes more
       const int ctx = b < p.B ? p.ctx_len[b] : 0;
-      return (ctx & pm) && p.new_len[b] > 0 ? p.block_table[(size_t)b * p.max_pages + (ctx >> sh)] : -1;
+      return (ctx & pm) && p.new_len[b] > 0 ? p.block_table[(size_t)b * p.max_pages + (ctx >> sh)] : 0;
     };
-    const int first = PART == PLAN_DROP ? goes_on(me) : -1;   // on its way beside the dropped ones
+    const int first = PART == PLAN_DROP ? goes_on(me) : 0;   // on its way beside the dropped ones
     for (uint32_t k = me; k < total[2]; k += all) {   // former requests' pages go above the stack's top
       const int b = find_row(s_gone, p.B, k);
       const int x = p.block_table[(size_t)b * p.max_pages + (k - s_gone[b])];
-      bad |= outside(x);
+      bad |= outside(x, -1);
       p.free_list[(uint32_t)n_free + k] = x;
     }
     if (PART == PLAN_ALL) {   // every page popped or gone on with is some token's
@@ -188,8 +192,9 @@ __global__ void __launch_bounds__(kPlanThreads) paged_plan_kernel(const PagedPla
       for (int u = 0; u < kMine; ++u) {
         const int t = tid + u * kPlanThreads;
         row[u] = pos[u] = id[u] = -1;
-        if ((uint32_t)t < total[0]) id[u] = token(t, row[u], pos[u]);
-        bad |= outside(id[u]);
+        bool dropped = true;
+        if ((uint32_t)t < total[0]) id[u] = token(t, row[u], pos[u], dropped);
+        bad |= outside(id[u], dropped ? -1 : 0);
       }
     } else {
       for (long long k = (long long)top - total[1] + me; k < n_free; k += all) bad |= outside(p.free_list[k]);
@@ -246,7 +251,8 @@ __global__ void __launch_bounds__(kPlanThreads) paged_plan_kernel(const PagedPla
   } else {
     for (int t = me; t < p.T; t += all) {
       int b = -1, at = -1;
-      const int page = (uint32_t)t < total[0] ? token(t, b, at) : -1;
+      bool dropped;
+      const int page = (uint32_t)t < total[0] ? token(t, b, at, dropped) : -1;
       put(t, b, at, page);
     }
   }
