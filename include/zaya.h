@@ -439,7 +439,8 @@ size_t zaya_paged_workspace_size(const zaya_config* cfg, int32_t B, int32_t T);
  *                   the prompts then attend over their bf16 keys and values
  *                   as in zaya_block_prefill, whatever kv_fp8.  0: every token
  *                   attends over the pages (kv_fp8: over the E4M3 values).
- *  state            keys and values go to slot_map; conv_state and prev_hs of
+ *  state            keys and values go to slot_map, where every row's token must
+ *                   have a slot of the pool; conv_state and prev_hs of
  *                   rows with new tokens move on (what they held is not read
  *                   where a row begins).
  *  taps             NULL or optional outputs, M = T (attention_queries bf16

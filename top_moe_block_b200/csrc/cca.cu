@@ -820,7 +820,7 @@ __global__ void __launch_bounds__(512) cca_ragged_kernel(const __grid_constant__
           i = t - first;
           pos = len - n + i;
           begins = len == n;
-          ok = first >= 0 && i >= 0 && i < n && len >= n && !(p.fresh && !begins);
+          ok = first >= 0 && i >= 0 && i < n && len >= n && !(p.fresh && !begins) && (unsigned)p.slot_map[t] < (unsigned)p.slots;
         }
         if (!ok) {
           set_status(p.status, ZAYA_ERR_DEVICE_RANGE);

@@ -244,6 +244,7 @@ struct CcaRaggedParams {
   const int* cu;          // [B + 1]
   const int* seq_len;     // [B]
   const int* token_row;   // [T]
+  const int* slot_map;    // [T]
   void* q_out;            // bf16 [T, n_q, d]
   void* tap_q;            // optional copy of q_out
   void* k_out;            // bf16 [T, n_kv, d]
@@ -255,6 +256,7 @@ struct CcaRaggedParams {
   const void* a_in;       // bf16 [T, H]
   int B, T, H, n_q, n_kv, d, rot;
   int cca_res, v_delayed;
+  int slots;              // of the pool: every row's token has one of them (checked)
   int fresh;              // 1: every row begins with this step (checked)
   float eps;
   int* status;
