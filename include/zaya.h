@@ -446,9 +446,9 @@ size_t zaya_paged_workspace_size(const zaya_config* cfg, int32_t B, int32_t T);
  *  taps             NULL or optional outputs, M = T (attention_queries bf16
  *                   [T, n_q, d]); rows behind the last one are unspecified.
  * conv_groups and kv_ring must be 0 (ZAYA_ERR_UNSUPPORTED).  B <= 4096, T < 2^24.  A
- * recorded fault leaves the state as it was, but for faults the attention
- * finds (block_table entries), which come after the new tokens' keys are
- * stored and the carried state has moved on. */
+ * recorded fault leaves the state as it was, but for block_table entries
+ * outside the pool and waits that run out, which come to light after the new
+ * tokens' keys are stored and the carried state has moved on. */
 int zaya_block_paged(const zaya_config* cfg, const zaya_block_weights* w, int32_t block_idx, int32_t B, int32_t T,
                      float* hidden, const int32_t* cu_new, const int32_t* seq_len, const int32_t* slot_map,
                      const int32_t* token_row, const int32_t* block_table, int32_t max_pages, int32_t fresh,

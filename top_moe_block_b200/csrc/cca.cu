@@ -808,6 +808,13 @@ __global__ void __launch_bounds__(512) cca_ragged_kernel(const __grid_constant__
                  : "memory");
   }
   asm volatile("cp.async.commit_group;" ::: "memory");
+  // The rows' lengths, what the attention will want of them included, so that a step with a wrong one
+  // stops before it moves any state; every CTA takes some rows.
+  for (int r = blockIdx.x * blockDim.x + threadIdx.x; r < p.B; r += gridDim.x * blockDim.x) {
+    const int first = p.cu[r], end = p.cu[r + 1], len = p.seq_len[r];
+    const bool off = (r == 0 && first < 0) || end < first || end > p.T || (!p.fresh && (len < end - first || len > p.room));
+    if (off) set_status(p.status, ZAYA_ERR_DEVICE_RANGE);
+  }
   if ((int)threadIdx.x < n_tok) {
     const int t = t0 + threadIdx.x;
     int b = -1, i = 0, pos = 0, begins = 0;
@@ -967,17 +974,14 @@ __global__ void __launch_bounds__(512) cca_ragged_kernel(const __grid_constant__
 }
 
 // conv_state and prev_hs of every row with new tokens move on to its last two
-// tokens (one CTA per row; rows that rest keep theirs).
+// tokens (one CTA per row; rows that rest keep theirs).  cca_ragged_kernel has
+// checked the lengths.
 __global__ void __launch_bounds__(256) carry_ragged_kernel(const __grid_constant__ CcaRaggedParams p) {
   griddep_begin();
   if (status_peek(p.status)) return;
   const int b = blockIdx.x;
   const int first = p.cu[b], n = p.cu[b + 1] - first;
   if (n <= 0) return;
-  if (first < 0 || p.cu[b + 1] > p.T) {
-    if (threadIdx.x == 0) set_status(p.status, ZAYA_ERR_DEVICE_RANGE);
-    return;
-  }
   const int C = (p.n_q + p.n_kv) * p.d, last = first + n - 1;
   const bool begins = p.seq_len[b] == n;
   const auto* x = static_cast<const __nv_bfloat16*>(p.qkv) + (size_t)last * p.n_qkv;

@@ -257,6 +257,7 @@ struct CcaRaggedParams {
   int B, T, H, n_q, n_kv, d, rot;
   int cca_res, v_delayed;
   int slots;              // of the pool: every row's token has one of them (checked)
+  int room;               // keys a row may have
   int fresh;              // 1: every row begins with this step (checked)
   float eps;
   int* status;

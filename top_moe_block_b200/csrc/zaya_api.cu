@@ -3,6 +3,7 @@
 // Declarations and the contract of every entry point are in zaya.h.
 #include <string.h>
 
+#include <algorithm>
 #include <atomic>
 #include <mutex>
 #include <vector>
@@ -634,6 +635,7 @@ int block_paged_impl(const zaya_config* cfg, const zaya_block_weights* w, int bl
   r.qkv = qkv; r.n_qkv = d.n_qkv; r.conv_w = w->conv_w; r.conv_b = w->conv_b; r.k_temp = w->k_temp;
   r.cu = cu; r.seq_len = seq_len; r.token_row = token_row;
   r.slot_map = slot_map; r.slots = state->kv.n_pages << sh;
+  r.room = fresh ? INT32_MAX : (int)std::min<long long>(1 << 30, (long long)max_pages << sh);
   r.q_out = q; r.tap_q = taps ? taps->attention_queries : nullptr; r.k_out = k; r.v_out = v; r.premix = premix;
   r.live = live; r.conv_state = state->conv_state; r.prev_hs = state->prev_hs; r.a_in = a_in;
   r.B = B; r.T = T; r.H = d.H; r.n_q = d.nq; r.n_kv = d.nkv; r.d = d.d; r.rot = c.rot_dim;
