@@ -36,7 +36,8 @@
 // a thread per query row (its TMEM lane); with E4M3 pages warps 12-15 expand the
 // raw tiles in their slots (exact), K to bf16 and V to f16.
 // P goes back over S, as bf16 (a weight off by up to 2^-8 of itself, while the sum
-// keeps the unrounded ones) or for E4M3 pages as f16, in two halves: the first
+// keeps the unrounded ones) or for E4M3 pages as f16 (2^-11 of itself, or 2^-32 of the
+// row's largest so far), in two halves: the first
 // half's product runs while the second's exponentials are taken.  O is rescaled
 // only when the running maximum grows by more than 2^8, which leaves the result
 // as it is.
@@ -86,6 +87,10 @@ constexpr float kRescaleLog2 = 8.0f;
 // is not rounded, so its distance from the rounded maximum is off by up to 2^-24
 // of the maximum, 2^-8 here.  Beyond it both are rounded alike.
 constexpr float kFusedMax = 65536.0f;
+// E4M3 pages: the running maximum is kept this far below the true one, so that the f16 weights lie
+// between 2^-24 and 2^(8 + 7) of it.  With its top at 1, weights under 2^-25 of the largest came to
+// nothing while the sum counted them: under one strong key, half of what 4000 others hold was lost.
+constexpr float kHeadroom = 7.0f;
 constexpr int kCvtWarps = 2;   // warps that expand an E4M3 tile together
 constexpr int kNoBox = -1;
 constexpr int kMaxLen = 1 << 30;   // keys of a row
@@ -901,11 +906,11 @@ __global__ void __launch_bounds__(Cfg<D, F8>::THREADS, 1)
           tmax = fmaxf(max3(mx[0], mx[1], tmax), fmaxf(mx[2], mx[3]));
         }
         // a NaN logit is no maximum, and spoils the sum below
-        const float m_new = fmaxf(m_used, tmax * sl2);
+        const float top = tmax * sl2, m_new = fmaxf(m_used, F8 && fabsf(top) < kFusedMax ? top - kHeadroom : top);
         // move the running maximum when it grew by more than 2^8, the whole
         // warp at once (the rescale is a warp-wide TMEM access); rows of no token, whose
         // logits may come from whatever lies behind the row's keys, have no say
-        if (__any_sync(0xffffffffu, valid && m_new > m_used + kRescaleLog2)) {
+        if (__any_sync(0xffffffffu, valid && m_new - m_used > kRescaleLog2)) {   // the difference is exact, a sum would not be
           const bool finite_new = m_new != -INFINITY;
           const float f = (m_used == -INFINITY || !finite_new) ? 1.f : exp2f(m_used - m_new);
           if (k > 0 && __any_sync(0xffffffffu, m_used != -INFINITY)) {
