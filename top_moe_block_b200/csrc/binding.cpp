@@ -36,42 +36,55 @@ struct Args {
     if (!ok) throw std::invalid_argument(std::string(name) + ": " + what + " on the current device is wanted");
   }
   bool local(const at::Tensor& t) const { return t.is_cuda() && t.get_device() == dev; }
-  const int32_t* ints(int i, const char* name, int64_t numel = -1) const {
+  const at::Tensor& words(int i, const char* name, int64_t numel) const {
     const at::Tensor& t = tensor(i, name);
     check(t.scalar_type() == at::kInt && local(t) && t.is_contiguous() && (numel < 0 || t.numel() == numel), name,
           numel < 0 ? "a contiguous int32 tensor" : "a contiguous int32 tensor of " + std::to_string(numel));
-    return static_cast<const int32_t*>(t.const_data_ptr());
+    return t;
   }
-  int32_t* ints_out(int i, const char* name, int64_t numel = -1) const { return const_cast<int32_t*>(ints(i, name, numel)); }
+  // What a call writes it takes through the mutable pointer, which gives a tensor that shares its
+  // storage until it is written (a lazy clone) a storage of its own.
+  const int32_t* ints(int i, const char* name, int64_t numel = -1) const {
+    return static_cast<const int32_t*>(words(i, name, numel).const_data_ptr());
+  }
+  int32_t* ints_out(int i, const char* name, int64_t numel = -1) const {
+    return static_cast<int32_t*>(words(i, name, numel).mutable_data_ptr());
+  }
   // [B, max_pages]
-  const int32_t* table(int i, int64_t B, int32_t* width) const {
-    const at::Tensor& t = tensor(i, "block_table");
+  const at::Tensor& table(int i, int64_t B, int32_t* width) const {
+    const at::Tensor& t = words(i, "block_table", -1);
     check(t.dim() == 2 && t.size(0) == B, "block_table", "int32 [" + std::to_string(B) + ", max_pages]");
     *width = count(t.size(1));
-    return ints(i, "block_table");
+    return t;
   }
   // bf16 [T, heads, d] with contiguous heads, tokens any stride apart
-  void* rows(int i, const char* name, int64_t T, int64_t heads, int64_t d, int32_t* stride) const {
+  const at::Tensor& rows_of(int i, const char* name, int64_t T, int64_t heads, int64_t d, int32_t* stride) const {
     const at::Tensor& t = tensor(i, name);
     check(t.scalar_type() == at::kBFloat16 && local(t) && t.dim() == 3 && t.size(0) == T && t.size(1) == heads &&
               t.size(2) == d && t.stride(2) == 1 && (heads == 1 || t.stride(1) == d),
           name, "bf16 [" + std::to_string(T) + ", " + std::to_string(heads) + ", " + std::to_string(d) + "] with contiguous heads");
     *stride = count(T > 1 ? t.stride(0) : heads * d);
-    return const_cast<void*>(t.const_data_ptr());
+    return t;
   }
-  void* plain(int i, const char* name, at::ScalarType type, std::initializer_list<int64_t> shape) const {
+  const void* rows(int i, const char* name, int64_t T, int64_t heads, int64_t d, int32_t* stride) const {
+    return rows_of(i, name, T, heads, d, stride).const_data_ptr();
+  }
+  void* rows_out(int i, const char* name, int64_t T, int64_t heads, int64_t d, int32_t* stride) const {
+    return rows_of(i, name, T, heads, d, stride).mutable_data_ptr();
+  }
+  const at::Tensor& plain(int i, const char* name, at::ScalarType type, std::initializer_list<int64_t> shape) const {
     const at::Tensor& t = tensor(i, name);
     std::string want;
     for (int64_t s : shape) want += (want.empty() ? "" : ", ") + std::to_string(s);
     check(t.scalar_type() == type && local(t) && t.is_contiguous() && t.sizes() == c10::IntArrayRef(shape), name,
           "a contiguous " + std::string(c10::toString(type)) + " [" + want + "]");
-    return const_cast<void*>(t.const_data_ptr());
+    return t;
   }
   void* workspace(int i, size_t* bytes) const {
     const at::Tensor& t = tensor(i, "workspace");
     check(local(t) && t.is_contiguous(), "workspace", "a contiguous tensor");
     *bytes = t.nbytes();
-    return const_cast<void*>(t.const_data_ptr());
+    return t.mutable_data_ptr();
   }
   static int32_t count(int64_t x) {
     if (x > INT32_MAX || x < INT32_MIN) throw std::invalid_argument("a size or stride is beyond 32 bits");
@@ -120,10 +133,10 @@ PyObject* paged_plan(PyObject*, PyObject* const* v, Py_ssize_t n) {
     const int64_t B = a.tensor(0, "ctx_len").numel(), T = a.tensor(10, "slot_map").numel();
     int32_t width;
     size_t bytes;
-    const int32_t* table = a.table(3, B, &width);
+    int32_t* table = static_cast<int32_t*>(a.table(3, B, &width).mutable_data_ptr());
     void* ws = a.workspace(13, &bytes);
     return zaya_paged_plan(Args::count(B), Args::count(T), a.ints(0, "ctx_len"), a.ints(1, "new_len", B),
-                           a.none(2) ? nullptr : a.ints(2, "drop_len", B), const_cast<int32_t*>(table), width,
+                           a.none(2) ? nullptr : a.ints(2, "drop_len", B), table, width,
                            a.ints_out(4, "free_list"), Args::count(a.tensor(4, "free_list").numel()), a.ints(5, "n_free_in", 1),
                            a.ints_out(6, "n_free_out", 1), a.integer(7), a.ints_out(8, "cu_new", B + 1),
                            a.ints_out(9, "seq_len", B), a.ints_out(10, "slot_map"), a.ints_out(11, "positions", T),
@@ -138,8 +151,8 @@ PyObject* paged_store(PyObject*, PyObject* const* v, Py_ssize_t n) {
     const int64_t T = a.tensor(3, "slot_map").numel();
     int32_t ks, vs;
     size_t bytes;
-    void* k = a.rows(1, "k", T, c->n_kv, c->head_dim, &ks);
-    void* val = a.rows(2, "v", T, c->n_kv, c->head_dim, &vs);
+    const void* k = a.rows(1, "k", T, c->n_kv, c->head_dim, &ks);
+    const void* val = a.rows(2, "v", T, c->n_kv, c->head_dim, &vs);
     void* ws = a.workspace(5, &bytes);
     return zaya_paged_store(c, Args::count(T), k, ks, val, vs, a.ints(3, "slot_map"), a.at_address<zaya_paged_kv>(4), ws,
                             bytes, a.stream(6));
@@ -153,9 +166,9 @@ PyObject* paged_attention(PyObject*, PyObject* const* v, Py_ssize_t n) {
     const int64_t B = a.tensor(4, "seq_len").numel(), T = a.tensor(2, "q").dim() ? a.tensor(2, "q").size(0) : 0;
     int32_t qs, os, width;
     size_t bytes;
-    void* q = a.rows(2, "q", T, c->n_q, c->head_dim, &qs);
-    void* out = a.rows(7, "out", T, c->n_q, c->head_dim, &os);
-    const int32_t* table = a.table(5, B, &width);
+    const void* q = a.rows(2, "q", T, c->n_q, c->head_dim, &qs);
+    void* out = a.rows_out(7, "out", T, c->n_q, c->head_dim, &os);
+    const auto* table = static_cast<const int32_t*>(a.table(5, B, &width).const_data_ptr());
     void* ws = a.workspace(8, &bytes);
     return zaya_paged_attention(c, a.integer(1), Args::count(B), Args::count(T), q, qs, a.ints(3, "cu_new", B + 1),
                                 a.ints(4, "seq_len"), table, width, a.at_address<zaya_paged_kv>(6), out, os, ws, bytes,
@@ -170,10 +183,10 @@ PyObject* packed_attention(PyObject*, PyObject* const* v, Py_ssize_t n) {
     const int64_t B = a.tensor(5, "cu_new").numel() - 1, T = a.tensor(2, "q").dim() ? a.tensor(2, "q").size(0) : 0;
     int32_t qs, ks, vs, os;
     size_t bytes;
-    void* q = a.rows(2, "q", T, c->n_q, c->head_dim, &qs);
-    void* k = a.rows(3, "k", T, c->n_kv, c->head_dim, &ks);
-    void* val = a.rows(4, "v", T, c->n_kv, c->head_dim, &vs);
-    void* out = a.rows(6, "out", T, c->n_q, c->head_dim, &os);
+    const void* q = a.rows(2, "q", T, c->n_q, c->head_dim, &qs);
+    const void* k = a.rows(3, "k", T, c->n_kv, c->head_dim, &ks);
+    const void* val = a.rows(4, "v", T, c->n_kv, c->head_dim, &vs);
+    void* out = a.rows_out(6, "out", T, c->n_q, c->head_dim, &os);
     void* ws = a.workspace(7, &bytes);
     return zaya_packed_attention(c, a.integer(1), Args::count(B), Args::count(T), q, qs, k, ks, val, vs,
                                  a.ints(5, "cu_new"), out, os, ws, bytes, a.stream(8));
@@ -190,11 +203,13 @@ PyObject* block_paged(PyObject*, PyObject* const* v, Py_ssize_t n) {
     size_t bytes;
     a.plain(13, "conv_state", at::kBFloat16, {B, int64_t(c->n_q + c->n_kv) * c->head_dim, 2});
     a.plain(14, "prev_hs", at::kBFloat16, {B, c->hidden});
-    const int32_t* table = a.table(8, B, &width);
+    const auto* table = static_cast<const int32_t*>(a.table(8, B, &width).const_data_ptr());
     void* ws = a.workspace(16, &bytes);
-    float* hidden = static_cast<float*>(a.plain(3, "hidden", at::kFloat, {T, c->hidden}));
-    const float* rin = a.none(10) ? nullptr : static_cast<float*>(a.plain(10, "router_state_in", at::kFloat, {T, c->router_hidden}));
-    float* rout = static_cast<float*>(a.plain(11, "router_state_out", at::kFloat, {T, c->router_hidden}));
+    float* hidden = static_cast<float*>(a.plain(3, "hidden", at::kFloat, {T, c->hidden}).mutable_data_ptr());
+    const float* rin = nullptr;
+    if (!a.none(10))
+      rin = static_cast<const float*>(a.plain(10, "router_state_in", at::kFloat, {T, c->router_hidden}).const_data_ptr());
+    float* rout = static_cast<float*>(a.plain(11, "router_state_out", at::kFloat, {T, c->router_hidden}).mutable_data_ptr());
     return zaya_block_paged(c, a.at_address<zaya_block_weights>(1), a.integer(2), Args::count(B), Args::count(T), hidden,
                             a.ints(4, "cu_new", B + 1), a.ints(5, "seq_len"), a.ints(6, "slot_map"), a.ints(7, "token_row", T),
                             table, width, a.integer(9), rin, rout, state, a.none(15) ? nullptr : a.at_address<zaya_taps>(15), ws,
