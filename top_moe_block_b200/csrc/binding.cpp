@@ -112,6 +112,16 @@ struct Args {
   }
 };
 
+// The C entry points run without the interpreter's lock, as through ctypes: a launch waits where
+// the device's queue is full.  What touches Python objects is done before.
+template <class F>
+int unlocked(F&& f) {
+  PyThreadState* st = PyEval_SaveThread();
+  const int rc = f();   // C: raises nothing
+  PyEval_RestoreThread(st);
+  return rc;
+}
+
 template <class F>
 PyObject* call(PyObject* const* v, Py_ssize_t n, Py_ssize_t want, F&& f) {
   if (n != want) {
@@ -135,12 +145,20 @@ PyObject* paged_plan(PyObject*, PyObject* const* v, Py_ssize_t n) {
     size_t bytes;
     int32_t* table = static_cast<int32_t*>(a.table(3, B, &width).mutable_data_ptr());
     void* ws = a.workspace(13, &bytes);
-    return zaya_paged_plan(Args::count(B), Args::count(T), a.ints(0, "ctx_len"), a.ints(1, "new_len", B),
-                           a.none(2) ? nullptr : a.ints(2, "drop_len", B), table, width,
-                           a.ints_out(4, "free_list"), Args::count(a.tensor(4, "free_list").numel()), a.ints(5, "n_free_in", 1),
-                           a.ints_out(6, "n_free_out", 1), a.integer(7), a.ints_out(8, "cu_new", B + 1),
-                           a.ints_out(9, "seq_len", B), a.ints_out(10, "slot_map"), a.ints_out(11, "positions", T),
-                           a.ints_out(12, "token_row", T), ws, bytes, a.stream(14));
+    const int32_t rows = Args::count(B), tokens = Args::count(T), n_pages = Args::count(a.tensor(4, "free_list").numel());
+    const int32_t *ctx = a.ints(0, "ctx_len"), *fresh = a.ints(1, "new_len", B);
+    const int32_t* drop = a.none(2) ? nullptr : a.ints(2, "drop_len", B);
+    int32_t* free_list = a.ints_out(4, "free_list");
+    const int32_t* n_in = a.ints(5, "n_free_in", 1);
+    int32_t* n_out = a.ints_out(6, "n_free_out", 1);
+    const int32_t page = a.integer(7);
+    int32_t *cu = a.ints_out(8, "cu_new", B + 1), *seq = a.ints_out(9, "seq_len", B), *slots = a.ints_out(10, "slot_map");
+    int32_t *pos = a.ints_out(11, "positions", T), *row = a.ints_out(12, "token_row", T);
+    void* stream = a.stream(14);
+    return unlocked([&] {
+      return zaya_paged_plan(rows, tokens, ctx, fresh, drop, table, width, free_list, n_pages, n_in, n_out, page, cu, seq, slots, pos,
+                             row, ws, bytes, stream);
+    });
   });
 }
 
@@ -154,8 +172,10 @@ PyObject* paged_store(PyObject*, PyObject* const* v, Py_ssize_t n) {
     const void* k = a.rows(1, "k", T, c->n_kv, c->head_dim, &ks);
     const void* val = a.rows(2, "v", T, c->n_kv, c->head_dim, &vs);
     void* ws = a.workspace(5, &bytes);
-    return zaya_paged_store(c, Args::count(T), k, ks, val, vs, a.ints(3, "slot_map"), a.at_address<zaya_paged_kv>(4), ws,
-                            bytes, a.stream(6));
+    const int32_t tokens = Args::count(T), *slots = a.ints(3, "slot_map");
+    const auto* kv = a.at_address<zaya_paged_kv>(4);
+    void* stream = a.stream(6);
+    return unlocked([&] { return zaya_paged_store(c, tokens, k, ks, val, vs, slots, kv, ws, bytes, stream); });
   });
 }
 
@@ -170,9 +190,13 @@ PyObject* paged_attention(PyObject*, PyObject* const* v, Py_ssize_t n) {
     void* out = a.rows_out(7, "out", T, c->n_q, c->head_dim, &os);
     const auto* table = static_cast<const int32_t*>(a.table(5, B, &width).const_data_ptr());
     void* ws = a.workspace(8, &bytes);
-    return zaya_paged_attention(c, a.integer(1), Args::count(B), Args::count(T), q, qs, a.ints(3, "cu_new", B + 1),
-                                a.ints(4, "seq_len"), table, width, a.at_address<zaya_paged_kv>(6), out, os, ws, bytes,
-                                a.stream(9));
+    const int32_t window = a.integer(1), rows = Args::count(B), tokens = Args::count(T);
+    const int32_t *cu = a.ints(3, "cu_new", B + 1), *seq = a.ints(4, "seq_len");
+    const auto* kv = a.at_address<zaya_paged_kv>(6);
+    void* stream = a.stream(9);
+    return unlocked([&] {
+      return zaya_paged_attention(c, window, rows, tokens, q, qs, cu, seq, table, width, kv, out, os, ws, bytes, stream);
+    });
   });
 }
 
@@ -188,8 +212,11 @@ PyObject* packed_attention(PyObject*, PyObject* const* v, Py_ssize_t n) {
     const void* val = a.rows(4, "v", T, c->n_kv, c->head_dim, &vs);
     void* out = a.rows_out(6, "out", T, c->n_q, c->head_dim, &os);
     void* ws = a.workspace(7, &bytes);
-    return zaya_packed_attention(c, a.integer(1), Args::count(B), Args::count(T), q, qs, k, ks, val, vs,
-                                 a.ints(5, "cu_new"), out, os, ws, bytes, a.stream(8));
+    const int32_t window = a.integer(1), rows = Args::count(B), tokens = Args::count(T), *cu = a.ints(5, "cu_new");
+    void* stream = a.stream(8);
+    return unlocked([&] {
+      return zaya_packed_attention(c, window, rows, tokens, q, qs, k, ks, val, vs, cu, out, os, ws, bytes, stream);
+    });
   });
 }
 
@@ -210,10 +237,16 @@ PyObject* block_paged(PyObject*, PyObject* const* v, Py_ssize_t n) {
     if (!a.none(10))
       rin = static_cast<const float*>(a.plain(10, "router_state_in", at::kFloat, {T, c->router_hidden}).const_data_ptr());
     float* rout = static_cast<float*>(a.plain(11, "router_state_out", at::kFloat, {T, c->router_hidden}).mutable_data_ptr());
-    return zaya_block_paged(c, a.at_address<zaya_block_weights>(1), a.integer(2), Args::count(B), Args::count(T), hidden,
-                            a.ints(4, "cu_new", B + 1), a.ints(5, "seq_len"), a.ints(6, "slot_map"), a.ints(7, "token_row", T),
-                            table, width, a.integer(9), rin, rout, state, a.none(15) ? nullptr : a.at_address<zaya_taps>(15), ws,
-                            bytes, a.stream(17));
+    const auto* weights = a.at_address<zaya_block_weights>(1);
+    const int32_t block = a.integer(2), rows = Args::count(B), tokens = Args::count(T), fresh = a.integer(9);
+    const int32_t *cu = a.ints(4, "cu_new", B + 1), *seq = a.ints(5, "seq_len"), *slots = a.ints(6, "slot_map");
+    const int32_t* row = a.ints(7, "token_row", T);
+    const auto* taps = a.none(15) ? nullptr : a.at_address<zaya_taps>(15);
+    void* stream = a.stream(17);
+    return unlocked([&] {
+      return zaya_block_paged(c, weights, block, rows, tokens, hidden, cu, seq, slots, row, table, width, fresh, rin, rout, state, taps,
+                              ws, bytes, stream);
+    });
   });
 }
 
