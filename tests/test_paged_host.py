@@ -165,3 +165,21 @@ def test_binding_checks_tensors():
         ZB.zaya_paged_attention(c, 8, q, i(3), i(2), i(2, 4), kv, q.clone(), ws)
     with pytest.raises(ValueError):
         ZB.zaya_packed_attention(c, 8, q, rows, rows, i(3), q.clone(), ws)
+
+
+def test_binding_is_rebuilt_for_another_torch_or_interpreter(tmp_path, monkeypatch):
+    assert build._fast_up_to_date()         # as the fixture left it
+    fast, stamp = tmp_path / "_fast.so", tmp_path / "_fast.stamp"
+    fast.write_bytes(b"")
+    monkeypatch.setattr(build, "FAST", str(fast))
+    monkeypatch.setattr(build, "FAST_STAMP", str(stamp))
+    assert not build._fast_up_to_date()     # a module of unknown origin
+    stamp.write_text(build._fast_stamp())
+    assert build._fast_up_to_date()
+    for change in (lambda m: m.setattr(torch, "__version__", "9.9.9"), lambda m: m.setattr(build, "_fast_flags", lambda: ["-O3"]),
+                   lambda m: m.setattr("sysconfig.get_config_var", lambda name: "cpython-999")):
+        with monkeypatch.context() as m:
+            change(m)
+            assert not build._fast_up_to_date()
+    os.utime(fast, (0, 0))
+    assert not build._fast_up_to_date()     # older than its source

@@ -15,6 +15,7 @@ HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
 OUT = os.path.join(HERE, "libzaya.so")
 FAST = os.path.join(HERE, "_fast.so")
+FAST_STAMP = os.path.join(HERE, "_fast.stamp")   # what _fast.so was built against
 BINDING = os.path.join(HERE, "csrc", "binding.cpp")
 
 
@@ -34,9 +35,26 @@ def up_to_date() -> bool:
     return all(os.path.getmtime(f) <= t for f in _deps())
 
 
+def _fast_flags() -> list[str]:
+    import torch
+    return ["-O2", "-std=c++17", "-fPIC", "-shared", f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}"]
+
+
+def _fast_stamp() -> str:
+    """The interpreter and the torch whose C++ interfaces _fast.so is compiled against, and the flags."""
+    import sysconfig
+
+    import torch
+    return "\n".join([sysconfig.get_config_var("SOABI") or sys.version, "torch " + torch.__version__,
+                      str(torch.version.git_version), " ".join(_fast_flags())]) + "\n"
+
+
 def _fast_up_to_date() -> bool:
-    if not os.path.exists(FAST):
+    if not os.path.exists(FAST) or not os.path.exists(FAST_STAMP):
         return False
+    with open(FAST_STAMP) as f:
+        if f.read() != _fast_stamp():
+            return False
     t = os.path.getmtime(FAST)
     return all(os.path.getmtime(f) <= t for f in [BINDING] + glob.glob(os.path.join(ROOT, "include", "*.h")))
 
@@ -49,8 +67,7 @@ def build_fast(verbose: bool = False) -> str:
     torch_dir = os.path.dirname(torch.__file__)
     cuda = os.path.dirname(os.path.dirname(shutil.which("nvcc") or "/usr/local/cuda/bin/nvcc"))
     tmp = FAST + ".tmp"
-    cmd = [shutil.which("g++") or "g++", "-O2", "-std=c++17", "-fPIC", "-shared",
-           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}"]
+    cmd = [shutil.which("g++") or "g++"] + _fast_flags()
     for d in (os.path.join(ROOT, "include"), os.path.join(torch_dir, "include"), os.path.join(cuda, "include"),
               sysconfig.get_paths()["include"]):
         cmd += ["-I", d]
@@ -60,6 +77,8 @@ def build_fast(verbose: bool = False) -> str:
         print(" ".join(cmd), file=sys.stderr)
     subprocess.run(cmd, check=True)
     os.replace(tmp, FAST)
+    with open(FAST_STAMP, "w") as f:
+        f.write(_fast_stamp())
     return FAST
 
 
