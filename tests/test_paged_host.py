@@ -4,6 +4,7 @@ touches a device, from the C ABI and from the Python binding."""
 import ctypes as C
 import os
 import subprocess
+import sys
 
 import pytest
 import torch
@@ -183,3 +184,14 @@ def test_binding_is_rebuilt_for_another_torch_or_interpreter(tmp_path, monkeypat
             assert not build._fast_up_to_date()
     os.utime(fast, (0, 0))
     assert not build._fast_up_to_date()     # older than its source
+
+
+def test_binding_that_does_not_load_says_why(tmp_path, monkeypatch):
+    monkeypatch.setattr(_abi, "_fast", None)
+    monkeypatch.delattr(ZB, "_fast", raising=False)
+    monkeypatch.setitem(sys.modules, "top_moe_block_b200._fast", None)     # stands for an undefined symbol
+    with pytest.raises(ImportError, match="does not load: import of top_moe_block_b200._fast halted"):
+        _abi.fast()
+    monkeypatch.setattr(_abi, "FAST_PATH", str(tmp_path / "_fast.so"))
+    with pytest.raises(ImportError, match="not built"):
+        _abi.fast()

@@ -8,6 +8,7 @@ import os
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "libzaya.so")
+FAST_PATH = os.path.join(_HERE, "_fast.so")
 
 ZAYA_OK = 0
 ZAYA_ERR_INVALID_ARG = 1
@@ -132,9 +133,11 @@ def fast():
     global _fast
     if _fast is None:
         lib()
+        if not os.path.exists(FAST_PATH):
+            raise ImportError(f"_fast.so not built ({FAST_PATH}); run top_moe_block_b200.build.build()")
         try:
             from . import _fast as module
         except ImportError as e:
-            raise ImportError("_fast.so not built; run top_moe_block_b200.build.build()") from e
+            raise ImportError(f"_fast.so does not load: {e}; run top_moe_block_b200.build.build(force=True)") from e
         _fast = module
     return _fast
