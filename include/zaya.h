@@ -398,7 +398,11 @@ size_t zaya_attention_workspace_size(const zaya_config* cfg);
  *  window       visible keys, the token's own included (> 0; 2^30: all).
  *  q, out       bf16 [T, n_q, d]; out must not overlap q.
  *  block_table  [B, max_pages]; pages before the window or behind the row's
- *               end are not read (their entries may hold anything).
+ *               end are not read (their entries may hold anything).  The host
+ *               knows no lengths: calls of few tokens take a kernel of less
+ *               latency where max_pages * page_size or the window is small (at
+ *               most 1024 keys), so a table no wider than the step's longest
+ *               row is faster; the two kernels round differently.
  * Keys no token of the row sees have no influence, whatever their bytes.  A
  * value that is not finite makes NaN of the tokens that see its key, and may
  * of tokens up to 255 positions before it and of those whose window it left

@@ -2,7 +2,7 @@
 // pipeline, whose chain from the lengths to the first output is 10 us.
 //
 // A CTA per (token, key head), a group of LPK lanes per key: the group's lanes hold
-// 16 or 32 bytes of a key row each, for all the query heads of the key head at once,
+// 8 to 32 bytes of a key row each, for all the query heads of the key head at once,
 // in fp32, weights included.  Every group runs over its own keys (every 32nd or so)
 // with a running maximum and sum, keys and values of BATCH of them on their way at a
 // time; the groups are added across the warp and then over the warps in shared memory,
@@ -21,24 +21,35 @@ namespace zaya {
 namespace {
 
 constexpr int kWarps = 8;
-// A call whose CTAs fit the SMs at once takes up to kOneWaveKeys keys a token, and up to
-// kOneWaveWork times query heads (4 heads: 64 rows x 251 keys 10.4 us against 20.7, 16 x 501
-// 14.9 against 17.3, but 2 x 901 23.3 against 16.9; 8 heads: 64 x 251 18.8 against 20.3, 64 x
-// 901 51.8 against 29.1).  Up to four times as many CTAs of small heads: up to kManyKeys.
-constexpr int kOneWaveKeys = 1024, kOneWaveWork = 2304, kManyKeys = 128;
-constexpr int kMaxPages = kOneWaveKeys / 16 + 1;
+// A call takes this kernel up to a number of keys that a token may see (the table's width or the
+// window, the less; the lengths are on the device).  Where its CTAs fit the SMs at once, by the query
+// heads of a key head: 1, 2, 4, 8 of 64, 8 of 128.  The border lies lower with few CTAs than where
+// most SMs have one, since there the other kernel's query tiles are cut.  Here against the other
+// kernel, us, bf16, one row: 1 head x 1000 keys 15.0 / 17.4; 2 x 500 11.7 / 16.8, x 1000 20.4 / 15.9;
+// 4 x 440 13.9 / 16.4, x 570 16.5 / 15.7; 8 of 64 x 280 12.7 / 14.2; 8 of 128 x 60 9.0 / 9.7,
+// x 80 10.5 / 10.0, x 280 20.8 / 15.5.  140 CTAs: 2 x 1000 25.6 / 31.2, 4 x 570 17.7 / 26.5, 8 of
+// 128 x 100 12.4 / 11.7, x 180 16.4 / 20.7, x 280 21.5 / 22.6.  E4M3: ahead wherever bf16 is.
+constexpr int kFewCtas[5] = {1024, 800, 560, 288, 72}, kMostCtas[5] = {1024, 1024, 576, 288, 288};
+// Up to four times as many CTAs of small heads (300 rows x 120 keys of 4 heads of 64: 11.4 / 17.6,
+// E4M3 11.0 / 19.6).
+constexpr int kManyKeys = 128;
+constexpr int kMaxPages = 1024 / 16 + 1;
 
 // N consecutive values of a key or value row as floats.
 template <int N, bool F8>
 struct Piece {
-  uint4 w[N * (F8 ? 1 : 2) / 16];
+  static constexpr int BYTES = N * (F8 ? 1 : 2);
+  alignas(BYTES < 16 ? BYTES : 16) uint32_t u[BYTES / 4];
   __device__ __forceinline__ void load(const void* base, size_t at) {
-    const uint4* s = reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(base) + at * (F8 ? 1 : 2));
+    const uint8_t* s = static_cast<const uint8_t*>(base) + at * (F8 ? 1 : 2);
+    if constexpr (BYTES == 8) {
+      *reinterpret_cast<uint2*>(u) = __ldcg(reinterpret_cast<const uint2*>(s));
+    } else {
 #pragma unroll
-    for (int i = 0; i < N * (F8 ? 1 : 2) / 16; ++i) w[i] = __ldcg(s + i);
+      for (int i = 0; i < BYTES / 16; ++i) reinterpret_cast<uint4*>(u)[i] = __ldcg(reinterpret_cast<const uint4*>(s) + i);
+    }
   }
   __device__ __forceinline__ void get(float (&x)[N]) const {
-    const uint32_t* u = reinterpret_cast<const uint32_t*>(w);
 #pragma unroll
     for (int i = 0; i < N; i += 2) {
       float2 f;
@@ -57,7 +68,8 @@ struct Piece {
 // BATCH: keys of a group under way at once; one, in fewer registers, where CTAs share an SM.
 template <int D, int REP, bool PAGED, bool F8, int BATCH>
 __global__ void __launch_bounds__(32 * kWarps, BATCH == 1 ? 3 : 1) attn_short_kernel(const __grid_constant__ RaggedAttnParams p) {
-  constexpr int DPL = (D == 128 && REP < 8) || F8 ? 16 : 8;   // dims of a lane
+  // dims of a lane: queries and outputs are 2 x REP x DPL registers
+  constexpr int DPL = REP < 8 && (D == 128 || (F8 && (BATCH > 1 || REP < 4))) ? 16 : 8;
   constexpr int LPK = D / DPL, KPW = 32 / LPK;                // lanes of a key, keys a warp takes at once
   constexpr int ROUND = kWarps * KPW;
   __shared__ int s_row, s_bad, s_page[kMaxPages];
@@ -251,7 +263,8 @@ bool attn_short_fits(const RaggedAttnParams& p, int num_sms) {
   const long long len = p.seq_len ? (long long)p.max_pages << p.page_shift : p.T;
   const long long keys = len < p.window ? len : p.window, ctas = (long long)p.T * p.n_kv;
   const int rep = p.n_q / p.n_kv;
-  if (ctas <= num_sms) return keys <= kOneWaveKeys && keys * rep <= kOneWaveWork;
+  const int heads = rep == 1 ? 0 : rep == 2 ? 1 : rep == 4 ? 2 : p.d == 64 ? 3 : 4;
+  if (ctas <= num_sms) return keys <= (ctas * 8 < num_sms * 7LL ? kFewCtas : kMostCtas)[heads];
   return ctas <= 4LL * num_sms && keys <= kManyKeys && p.d * rep <= 256;
 }
 
