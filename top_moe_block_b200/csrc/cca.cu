@@ -809,8 +809,9 @@ __global__ void __launch_bounds__(512) cca_ragged_kernel(const __grid_constant__
   }
   asm volatile("cp.async.commit_group;" ::: "memory");
   // The rows' lengths, what the attention will want of them included, so that a step with a wrong one
-  // stops before it moves any state; every CTA takes some rows.
-  for (int r = blockIdx.x * blockDim.x + threadIdx.x; r < p.B; r += gridDim.x * blockDim.x) {
+  // stops before it moves any state; every CTA takes some rows, from its last warp on (the first has
+  // the tokens).
+  for (int r = blockIdx.x * blockDim.x + blockDim.x - 1 - threadIdx.x; r < p.B; r += gridDim.x * blockDim.x) {
     const int first = p.cu[r], end = p.cu[r + 1], len = p.seq_len[r];
     const bool off = (r == 0 && first < 0) || end < first || end > p.T || (!p.fresh && (len < end - first || len > p.room));
     if (off) set_status(p.status, ZAYA_ERR_DEVICE_RANGE);
@@ -819,15 +820,16 @@ __global__ void __launch_bounds__(512) cca_ragged_kernel(const __grid_constant__
     const int t = t0 + threadIdx.x;
     int b = -1, i = 0, pos = 0, begins = 0;
     if (t < p.T) {
-      if (t < p.cu[p.B]) {
-        b = p.token_row[t];
-        bool ok = (unsigned)b < (unsigned)p.B;
+      const int end = p.cu[p.B], row = p.token_row[t], slot = p.slot_map[t];   // on their way together
+      if (t < end) {
+        b = row;
+        bool ok = (unsigned)b < (unsigned)p.B && (unsigned)slot < (unsigned)p.slots;
         if (ok) {
           const int first = p.cu[b], n = p.cu[b + 1] - first, len = p.seq_len[b];
           i = t - first;
           pos = len - n + i;
           begins = len == n;
-          ok = first >= 0 && i >= 0 && i < n && len >= n && !(p.fresh && !begins) && (unsigned)p.slot_map[t] < (unsigned)p.slots;
+          ok = first >= 0 && i >= 0 && i < n && len >= n && !(p.fresh && !begins);
         }
         if (!ok) {
           set_status(p.status, ZAYA_ERR_DEVICE_RANGE);
