@@ -311,7 +311,8 @@ int zaya_stack_forward(const zaya_config* cfg, int32_t n_blocks, const zaya_bloc
  * Serving steps over requests of different lengths, without padding: a step
  * holds B rows (requests) of 0 or more new tokens each, packed one row after
  * the other in arrays of T tokens (cu_new[b] is row b's first token; tokens
- * from cu_new[B] on belong to no row and are neither read nor written), and
+ * from cu_new[B] on belong to no row and are neither read nor written, but
+ * for hidden and router state in zaya_block_paged), and
  * the cache is a pool of pages, found through one block table per row.  The
  * pages' deployments serve the model this way (a serving engine with an fp8
  * KV cache: NVFP4 README, "Throughput and memory").
@@ -404,9 +405,14 @@ size_t zaya_attention_workspace_size(const zaya_config* cfg);
  *               most 1024 keys), so a table no wider than the step's longest
  *               row is faster; the two kernels round differently.
  * Keys no token of the row sees have no influence, whatever their bytes.  A
- * value that is not finite makes NaN of the tokens that see its key, and may
- * of tokens up to 255 positions before it and of those whose window it left
- * up to 255 positions ago.  seq_len is at most 2^30.  The same call gives the
+ * value that is not finite makes the outputs of tokens that see its key not
+ * finite, and may those of tokens up to 255 positions before it and of those
+ * whose window it left up to 255 positions ago; a logit that is NaN or +inf
+ * makes NaN, one of -inf weighs nothing.  Logits, maxima, sums and outputs are
+ * fp32; each weight is rounded once for its product with the values (but not
+ * in its sum), by at most 2^-8 of itself to bf16, or over E4M3 pages by 2^-11
+ * of itself or 2^-32 of the row's largest to f16; calls of few tokens over few
+ * keys keep fp32 weights.  seq_len is at most 2^30.  The same call gives the
  * same bits every time. */
 int zaya_paged_attention(const zaya_config* cfg, int32_t window, int32_t B, int32_t T, const void* q,
                          int32_t q_stride, const int32_t* cu_new, const int32_t* seq_len,

@@ -45,13 +45,15 @@
 // What bounds it (times of calls in a row, 8 query and 2 key heads of 128):
 //   long prompts and chunks: the lane's cycle of softmax and MMAs (tensor pipe 46 %
 //     busy at 16k keys, special-function unit 46 %, about 5 cycles an
-//     instruction).  8192 tokens after 24576: 0.87 to 0.92 ms (1.05 to 1.1
-//     PFLOP/s; the card is at its power limit); a prompt of 4096: 62 us.
-//   decoding: the HBM, once the pipe is full.  64 rows, window 4096: 61 us (4.4 TB/s
-//     with its start and end; 1.6 us a key tile between them, 6 TB/s), E4M3 70 us
-//     (the expansion's instructions and shared-memory traffic).
+//     instruction).  8192 tokens after 24576: 0.92 to 0.98 ms (0.98 to 1.04
+//     PFLOP/s; the card is at its power limit); a prompt of 4096: 59 us.
+//     E4M3 pages: 1.05 ms for the chunk, 81 us for 12 ragged ones (bf16 72).
+//   decoding: the HBM, once the pipe is full.  64 rows, window 4096: 61 to 64 us (4.2 to
+//     4.4 TB/s with its start and end; 1.6 us a key tile between them, 6 TB/s), E4M3
+//     71 us (the expansion's instructions and shared-memory traffic).
 //   small calls: the chain of dependent steps (lengths, share, page ids, first
-//     tile, softmax, output), 10 to 12 us.
+//     tile, softmax, output), 10 us for one row over 31 keys, 21 for 64 over 250
+//     (128 query tiles, which 148 shares cut).
 // Code size counts: with few warps and many roles, straight-line code waits for
 // its instructions.  Loops over halves of a tile that read S twice beat one pass
 // over all of it with S in registers (decode 65 -> 61 us, E4M3 77 -> 72 us), E4M3
@@ -76,10 +78,14 @@ constexpr int kRows = 128;   // query rows of an MMA tile
 constexpr int kKeys = 128;   // keys of a key tile
 constexpr int kMaxCtas = ZAYA_ATTENTION_CLEAR / 16;   // four counters each
 constexpr int kFlat = 4;     // CTAs of a query tile up to which one of them merges all
-constexpr int kMinShare = 8; // weight a CTA takes at least: below one short query tile's, so that short rows are not
-                             // put together (7 short prompts 12.5 us; with 12 they take 14.8, a lone 32k decode 24.0 for 24.9)
-// What a key tile costs a query tile of up to 128 rows, and of more (measured: 1.6 to 1.9 us,
-// bound by the loads, against 2.3); and what a query tile costs beside its key tiles.
+// Weight a CTA takes at least: below one short query tile's, so that short rows are not put together.
+// Decoding calls with 8, 12 and 16 (us): 1 row x 31 keys 10.4, 15.1, 15.1; 1 x 1100 15.4, 18.7, 19.2;
+// 4 x 300 15.5, 18.1, 20.9; 16 x 1100 18.2, 19.7, 22.3.  12 is ahead for 1 x 32768 (24.2, 22.9, 25.7) and
+// 64 x 250 (20.8, 15.4, 21.7).
+constexpr int kMinShare = 8;
+// What a key tile costs a query tile of up to 128 rows, and of more (measured over bf16 pages with 8
+// query and 2 key heads of 128: 1.6 to 1.9 us, bound by the loads, against 2.3; used for every head
+// and page type); and what a query tile costs beside its key tiles.
 constexpr int kKeyCost = 3, kKeyCostTwo = 4, kTileCost = 6;
 constexpr int kSegs = 4;     // ring of segments
 constexpr float kRescaleLog2 = 8.0f;
